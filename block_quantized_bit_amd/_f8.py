@@ -6,7 +6,7 @@ import ctypes
 import torch
 
 from ._args import device_of, dtype_of, native, pointer
-from ._lib import _check, _stream, lib
+from ._lib import _check, _empty, _stream, lib
 
 F8 = torch.float8_e4m3fn
 F8_EXPORTS = ("f8_quantize_rows", "f8_quantize_cols", "f8_quantize_weights", "f8_transpose_weights", "f8_gemm",
@@ -52,8 +52,8 @@ def f8_quantize_act(x: torch.Tensor, stream=None):
     Kp = K rounded up to 128: one scale for each 1 x 128 block."""
     dev, dt, M, K, px, stride = _rows(x, "x")
     kb = _blocks(K)
-    xq = torch.empty((M, kb * 128), dtype=F8, device=x.device)
-    xs = torch.empty((kb, M), dtype=torch.float32, device=x.device)
+    xq = _empty(stream, (M, kb * 128), F8, x.device)
+    xs = _empty(stream, (kb, M), torch.float32, x.device)
     _check(_f8().f8_quantize_rows(M, K, dt, px, stride, xq.data_ptr(), xs.data_ptr(), _stream(stream)),
            "f8_quantize_rows")
     return xq, xs
@@ -64,8 +64,8 @@ def f8_quantize_act_t(x: torch.Tensor, stream=None):
     of 128 tokens (the weight gradient's operands)."""
     dev, dt, M, K, px, stride = _rows(x, "x")
     mb = _blocks(M)
-    xt = torch.empty((K, mb * 128), dtype=F8, device=x.device)
-    xts = torch.empty((mb, K), dtype=torch.float32, device=x.device)
+    xt = _empty(stream, (K, mb * 128), F8, x.device)
+    xts = _empty(stream, (mb, K), torch.float32, x.device)
     _check(_f8().f8_quantize_cols(M, K, dt, px, stride, xt.data_ptr(), xts.data_ptr(), _stream(stream)),
            "f8_quantize_cols")
     return xt, xts
@@ -77,8 +77,8 @@ def f8_quantize_weights(w: torch.Tensor, stream=None):
     dt = dtype_of(w, "w")
     N, K = w.shape
     pw = pointer(w, dev, (N, K), w.dtype, "w")
-    wq = torch.empty((N, _blocks(K) * 128), dtype=F8, device=w.device)
-    ws = torch.empty((_blocks(N), _blocks(K)), dtype=torch.float32, device=w.device)
+    wq = _empty(stream, (N, _blocks(K) * 128), F8, w.device)
+    ws = _empty(stream, (_blocks(N), _blocks(K)), torch.float32, w.device)
     _check(_f8().f8_quantize_weights(N, K, dt, pw, wq.data_ptr(), ws.data_ptr(), _stream(stream)),
            "f8_quantize_weights")
     return wq, ws
@@ -92,8 +92,8 @@ def f8_transpose_weights(wq: torch.Tensor, ws: torch.Tensor, K: int, stream=None
     kb, nb = _blocks(K), _blocks(N)
     pq = pointer(wq, dev, (N, kb * 128), F8, "wq")
     ps = pointer(ws, dev, (nb, kb), torch.float32, "ws")
-    wqt = torch.empty((K, nb * 128), dtype=F8, device=wq.device)
-    wst = torch.empty((kb, nb), dtype=torch.float32, device=wq.device)
+    wqt = _empty(stream, (K, nb * 128), F8, wq.device)
+    wst = _empty(stream, (kb, nb), torch.float32, wq.device)
     _check(_f8().f8_transpose_weights(N, K, pq, ps, wqt.data_ptr(), wst.data_ptr(), _stream(stream)),
            "f8_transpose_weights")
     return wqt, wst
@@ -105,7 +105,7 @@ def f8_gemm(xq, xs, wq, ws, out=None, dtype=torch.float32, stream=None):
     M, Kp = xq.shape
     N, kb = wq.shape[0], _blocks(Kp)
     if out is None:
-        out = torch.empty((M, N), dtype=dtype, device=xq.device)
+        out = _empty(stream, (M, N), dtype, xq.device)
     _check(_f8().f8_gemm(M, Kp, N, dtype_of(out, "out"), pointer(xq, dev, (M, Kp), F8, "xq"),
                          pointer(xs, dev, (kb, M), torch.float32, "xs"), pointer(wq, dev, (N, Kp), F8, "wq"),
                          pointer(ws, dev, (_blocks(N), kb), torch.float32, "ws"),

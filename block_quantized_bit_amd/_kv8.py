@@ -8,6 +8,7 @@ from __future__ import annotations
 import torch
 
 from ._args import native
+from ._lib import _empty
 
 KV8_EXPORTS = ("kv8_append", "kv8_read", "kv8_attention_work_bytes", "kv8_attention")
 KV8_DTYPES = (torch.int8, torch.float8_e4m3fn)
@@ -37,7 +38,7 @@ def kv8_read(k_codes, v_codes, k_scale, v_scale, page_table, kv_len, cu, max_new
         if total is None:
             raise ValueError("total (the last entry of cu) or out is needed")
         shape = (total, k_codes.shape[1], k_codes.shape[3])
-        out = tuple(torch.empty(shape, dtype=dtype, device=k_codes.device) for _ in range(2))
+        out = tuple(_empty(stream, shape, dtype, k_codes.device) for _ in range(2))
     native().kv8_read(k_codes, v_codes, k_scale, v_scale, page_table, kv_len, cu, max_new, out[0], out[1], stream)
     return out[0], out[1]
 

@@ -100,6 +100,17 @@ def _stream(stream=None):
     return ctypes.c_void_p(s.cuda_stream)
 
 
+def _empty(stream, shape, dtype, device):
+    """A new tensor for a call on `stream` (None: the current one). It belongs to that stream, as if the call stood under
+    torch.cuda.stream(stream): the allocator hands its memory on to later work of that stream only."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(stream.cuda_stream, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
 def _check(rc: int, what: str):
     if rc != 0:
         raise Q4Error(rc, what)

@@ -71,15 +71,37 @@ c10::Device device_of(const at::Tensor& t, const char* what) {
     return d;
 }
 
-void* stream_of(PyObject* stream, c10::Device dev) {
-    if (none(stream)) return c10::hip::getCurrentHIPStream(dev.index()).stream();
-    PyObject* h = PyObject_GetAttrString(stream, "cuda_stream");
-    if (!h) throw PythonProblem();
-    void* p = PyLong_AsVoidPtr(h);
-    Py_DECREF(h);
-    if (!p && PyErr_Occurred()) throw PythonProblem();
-    return p;
-}
+// The stream of a call: the current one, or the one given (any object with a `cuda_stream` handle), which is then the
+// current one while this lives. Workspaces and results that the call allocates so belong to the stream that uses them:
+// the allocator may hand a workspace's memory on as soon as the call returns, but only to later work of that stream.
+class OnStream {
+  public:
+    OnStream(PyObject* stream, c10::Device dev) : before_(c10::hip::getCurrentHIPStream(dev.index())) {
+        if (none(stream)) {
+            handle = before_.stream();
+            return;
+        }
+        PyObject* h = PyObject_GetAttrString(stream, "cuda_stream");
+        if (!h) throw PythonProblem();
+        handle = PyLong_AsVoidPtr(h);
+        Py_DECREF(h);
+        if (!handle && PyErr_Occurred()) throw PythonProblem();
+        if (handle == before_.stream()) return;
+        c10::hip::setCurrentHIPStream(c10::hip::getStreamFromExternal((hipStream_t)handle, dev.index()));
+        moved_ = true;
+    }
+    ~OnStream() {
+        if (moved_) c10::hip::setCurrentHIPStream(before_);
+    }
+    OnStream(const OnStream&) = delete;
+    OnStream& operator=(const OnStream&) = delete;
+
+    void* handle;
+
+  private:
+    c10::hip::HIPStream before_;
+    bool moved_ = false;
+};
 
 int dtype_of(const at::Tensor& t, const char* what) {
     if (t.scalar_type() == at::kFloat) return Q4_DT_F32;
@@ -173,6 +195,7 @@ PyObject* linear(PyObject*, PyObject* const* a, Py_ssize_t) {
     return guarded([&]() -> PyObject* {
         const at::Tensor &x = tensor(a[0], "x"), &wq = tensor(a[1], "wq");
         const c10::Device dev = device_of(x, "x");
+        const OnStream on(a[5], dev);
         const Rows r = rows_of(x, dev, "x");
         if (wq.dim() != 2) bad("wq: expected [N][K padded to 128]");
         const int64_t N = wq.size(0), Kp = up128(r.K);
@@ -182,7 +205,7 @@ PyObject* linear(PyObject*, PyObject* const* a, Py_ssize_t) {
         void* po = pointer(out, dev, {r.M, N}, x.scalar_type(), "out");
         const at::Tensor work = workspace(a[4], f8_linear_work_bytes((int)r.M, (int)r.K), dev);
         check(f8_linear((int)r.M, (int)r.K, (int)N, r.dtype, r.p, r.stride, (const uint8_t*)pq, (const float*)ps, po,
-                        work.data_ptr(), stream_of(a[5], dev)),
+                        work.data_ptr(), on.handle),
               "f8_linear");
         return THPVariable_Wrap(out);
     });
@@ -193,6 +216,7 @@ PyObject* linear_backward(PyObject*, PyObject* const* a, Py_ssize_t) {
     return guarded([&]() -> PyObject* {
         const at::Tensor& dy = tensor(a[0], "dy");
         const c10::Device dev = device_of(dy, "dy");
+        const OnStream on(a[9], dev);
         const Rows d = rows_of(dy, dev, "dy");
         const bool need_dx = PyObject_IsTrue(a[6]) == 1, need_dw = PyObject_IsTrue(a[7]) == 1;
         const auto type = dy.scalar_type();
@@ -221,7 +245,7 @@ PyObject* linear_backward(PyObject*, PyObject* const* a, Py_ssize_t) {
         const at::Tensor work = workspace(a[8], f8_linear_backward_work_bytes((int)d.M, (int)x.K, (int)d.K), dev);
         check(f8_linear_backward((int)d.M, (int)x.K, (int)d.K, d.dtype, d.p, d.stride, x.p, x.stride,
                                  (const uint8_t*)pq, (const float*)ps, pdx, dwtype, pdw, work.data_ptr(),
-                                 stream_of(a[9], dev)),
+                                 on.handle),
               "f8_linear_backward");
         PyObject* first = need_dx ? THPVariable_Wrap(dx) : (Py_INCREF(Py_None), Py_None);
         PyObject* second = need_dw ? THPVariable_Wrap(dw) : (Py_INCREF(Py_None), Py_None);
@@ -283,12 +307,13 @@ PyObject* append(PyObject*, PyObject* const* a, Py_ssize_t) {
     return guarded([&]() -> PyObject* {
         kv8_cache c;
         const c10::Device dev = cache_of(a + 2, c);
+        const OnStream on(a[10], dev);
         const at::Tensor &k = tensor(a[0], "k"), &v = tensor(a[1], "v");
         const int64_t ks = tokens_of(k, dev, c.kv_heads, c.head_dim, "k");
         const int64_t vs = tokens_of(v, dev, c.kv_heads, c.head_dim, "v");
         if (v.scalar_type() != k.scalar_type() || v.size(0) != k.size(0)) bad("k and v disagree on dtype or tokens");
         check(kv8_append(&c, (int)k.size(0), (int)integer(a[9], "max_new"), dtype_of(k, "k"), k.data_ptr(), ks,
-                         v.data_ptr(), vs, stream_of(a[10], dev)),
+                         v.data_ptr(), vs, on.handle),
               "kv8_append");
         Py_RETURN_NONE;
     });
@@ -299,12 +324,13 @@ PyObject* read(PyObject*, PyObject* const* a, Py_ssize_t) {
     return guarded([&]() -> PyObject* {
         kv8_cache c;
         const c10::Device dev = cache_of(a, c);
+        const OnStream on(a[10], dev);
         const at::Tensor &k = tensor(a[8], "out[0]"), &v = tensor(a[9], "out[1]");
         const int dt = dtype_of(k, "out[0]");
         if (k.dim() != 3 || k.size(0) < 1 || k.size(0) > 0x7FFFFFFF) bad("out[0]: expected [tokens][kv heads][head size]");
         void* pk = pointer(k, dev, {k.size(0), c.kv_heads, c.head_dim}, k.scalar_type(), "out[0]");
         void* pv = pointer(v, dev, {k.size(0), c.kv_heads, c.head_dim}, k.scalar_type(), "out[1]");
-        check(kv8_read(&c, (int)k.size(0), (int)integer(a[7], "max_new"), dt, pk, pv, stream_of(a[10], dev)), "kv8_read");
+        check(kv8_read(&c, (int)k.size(0), (int)integer(a[7], "max_new"), dt, pk, pv, on.handle), "kv8_read");
         Py_RETURN_NONE;
     });
 }
@@ -314,6 +340,7 @@ PyObject* attention(PyObject*, PyObject* const* a, Py_ssize_t) {
     return guarded([&]() -> PyObject* {
         kv8_cache c;
         const c10::Device dev = cache_of(a + 1, c);
+        const OnStream on(a[15], dev);
         const at::Tensor& q = tensor(a[0], "q");
         if (q.dim() != 3) bad("q: expected [tokens][heads][head size]");
         const int64_t total = q.size(0), heads = q.size(1), D = c.head_dim;
@@ -336,7 +363,7 @@ PyObject* attention(PyObject*, PyObject* const* a, Py_ssize_t) {
         const at::Tensor work =
             workspace(a[14], kv8_attention_work_bytes(&c, (int)total, max_new, max_kv, (int)heads), dev);
         check(kv8_attention(&c, (int)total, max_new, max_kv, (int)heads, dt, q.data_ptr(), stride, (float)scale, window,
-                            po, lse, work.data_ptr(), stream_of(a[15], dev)),
+                            po, lse, work.data_ptr(), on.handle),
               "kv8_attention");
         return THPVariable_Wrap(out);
     });
@@ -349,6 +376,7 @@ PyObject* moe(PyObject*, PyObject* const* a, Py_ssize_t) {
     return guarded([&]() -> PyObject* {
         const at::Tensor &x = tensor(a[0], "x"), &logits = tensor(a[1], "logits"), &w13 = tensor(a[2], "w13");
         const c10::Device dev = device_of(x, "x");
+        const OnStream on(a[14], dev);
         const int dt = dtype_of(x, "x");
         if (x.dim() != 2 || logits.dim() != 2 || w13.dim() != 3)
             bad("expected x [T][H], logits [T][E], w13 [E][2I][H/2]");
@@ -376,7 +404,7 @@ PyObject* moe(PyObject*, PyObject* const* a, Py_ssize_t) {
             workspace(a[13], moe_q4_work_bytes((int)T, (int)H, (int)I, (int)E, top_k, bs), dev);
         check(moe_q4((int)T, (int)H, (int)I, (int)E, top_k, bs, fmt, dt, px, (const float*)pl, (const uint8_t*)p13, ps13,
                      pb13, (const uint8_t*)p2, ps2, pb2, PyObject_IsTrue(a[11]) == 1, po, work.data_ptr(),
-                     stream_of(a[14], dev)),
+                     on.handle),
               "moe_q4");
         return THPVariable_Wrap(out);
     });
