@@ -138,9 +138,9 @@ def quantize_act(x: torch.Tensor, bs: int, out=None, stream=None):
     """x [M][K] float32 or bfloat16 -> (xq int8 [M][K], xs float32 [M][K/bs], xsum int32 [M][K/bs])."""
     M, K = x.shape
     if out is None:
-        xq = torch.empty((M, K), dtype=torch.int8, device=x.device)
-        xs = torch.empty((M, K // bs), dtype=torch.float32, device=x.device)
-        xsum = torch.empty((M, K // bs), dtype=torch.int32, device=x.device)
+        xq = _empty(stream, (M, K), torch.int8, x.device)
+        xs = _empty(stream, (M, K // bs), torch.float32, x.device)
+        xsum = _empty(stream, (M, K // bs), torch.int32, x.device)
     else:
         xq, xs, xsum = out
     _check(lib().q4_quantize_act(M, K, bs, _xdtype(x), _ptr(x), _ptr(xq), _ptr(xs), _ptr(xsum), _stream(stream)),
@@ -167,7 +167,7 @@ def _matmul(entry: str, M: int, fmt: str, bs: int, wq, wscale, wbias, xq, xs, xs
 def gemv(fmt: str, bs: int, wq, wscale, wbias, xq, xs, xsum, y=None, bits: int = 4, stream=None):
     """Decode GEMV (xq is [1][K]) -> y float32 [1][N]."""
     if y is None:
-        y = torch.empty((xq.shape[0], wscale.shape[0]), dtype=torch.float32, device=wq.device)
+        y = _empty(stream, (xq.shape[0], wscale.shape[0]), torch.float32, wq.device)
     return _matmul("q4_gemv", xq.shape[0], fmt, bs, wq, wscale, wbias, xq, xs, xsum, y, bits, stream)
 
 
@@ -179,7 +179,7 @@ def gemv_fused(fmt: str, bs: int, x, wq, wscale, wbias, y=None, act_out=None, bi
     if x.shape[1] != K:
         raise ValueError("x and wq disagree on K")
     if y is None:
-        y = torch.empty((x.shape[0], N), dtype=torch.float32, device=wq.device)
+        y = _empty(stream, (x.shape[0], N), torch.float32, wq.device)
     xq, xs, xsum = act_out if act_out is not None else (None, None, None)
     _check(lib().q4_gemv_fused(x.shape[0], K, N, bs, _fmt(fmt), bits, _xdtype(x), _ptr(x), _ptr(wq), _ptr(wscale),
                                _ptr(wbias), _ptr(y), _ptr(xq), _ptr(xs), _ptr(xsum), _stream(stream)),
@@ -190,7 +190,7 @@ def gemv_fused(fmt: str, bs: int, x, wq, wscale, wbias, y=None, act_out=None, bi
 def gemm(fmt: str, bs: int, wq, wscale, wbias, xq, xs, xsum, y=None, bits: int = 4, stream=None):
     """Prefill GEMM (xq is [M][K]) -> y float32 [M][N]."""
     if y is None:
-        y = torch.empty((xq.shape[0], wscale.shape[0]), dtype=torch.float32, device=wq.device)
+        y = _empty(stream, (xq.shape[0], wscale.shape[0]), torch.float32, wq.device)
     return _matmul("q4_gemm", xq.shape[0], fmt, bs, wq, wscale, wbias, xq, xs, xsum, y, bits, stream)
 
 
@@ -202,7 +202,7 @@ def debug_partials(path: str, fmt: str, bs: int, wq, xq, xsum, m0: int = 0, m1: 
     N = wq.numel() * 8 // (K * bits)
     m1 = M if m1 is None else m1
     if out is None:
-        out = torch.empty((max(m1 - m0, 1), N, K // bs), dtype=torch.int32, device=wq.device)
+        out = _empty(stream, (max(m1 - m0, 1), N, K // bs), torch.int32, wq.device)
     p = {"gemv": Q4_PATH_GEMV, "gemm": Q4_PATH_GEMM, "small": Q4_PATH_SMALL}[path]
     _check(lib().q4_debug_partials(p, M, K, N, bs, _fmt(fmt), bits, _ptr(wq), _ptr(xq), _ptr(xsum), m0, m1,
                                    _ptr(out), _stream(stream)), "q4_debug_partials")
@@ -214,7 +214,7 @@ def debug_partials_fused(fmt: str, bs: int, x, wq, out=None, bits: int = 4, stre
     K = x.shape[1]
     N = wq.numel() * 8 // (K * bits)
     if out is None:
-        out = torch.empty((N, K // bs), dtype=torch.int32, device=wq.device)
+        out = _empty(stream, (N, K // bs), torch.int32, wq.device)
     _check(lib().q4_debug_partials_fused(K, N, bs, _fmt(fmt), bits, _xdtype(x), _ptr(x), _ptr(wq), _ptr(out),
                                          _stream(stream)), "q4_debug_partials_fused")
     return out
@@ -232,7 +232,7 @@ def pack_weights(fmt: str, bs: int, wq, wscale, wbias, bits: int = 4, stream=Non
     nbytes = packed_bytes(K, N, bs, fmt)
     if nbytes == 0:
         raise ValueError("invalid shape or format for packing")
-    packed = torch.empty(nbytes, dtype=torch.uint8, device=wq.device)
+    packed = _empty(stream, nbytes, torch.uint8, wq.device)
     _check(lib().q4_pack_weights(N, K, bs, _fmt(fmt), bits, _ptr(wq), _ptr(wscale), _ptr(wbias), _ptr(packed),
                                  _stream(stream)), "q4_pack_weights")
     return packed
@@ -247,9 +247,9 @@ def gemm_packed(fmt: str, bs: int, x, packed, N: int, y=None, work=None, bits: i
     if wbytes == 0:
         raise ValueError("invalid shape for the packed GEMM")
     if y is None:
-        y = torch.empty((M, N), dtype=torch.float32, device=x.device)
+        y = _empty(stream, (M, N), torch.float32, x.device)
     if work is None:
-        work = torch.empty(wbytes, dtype=torch.uint8, device=x.device)
+        work = _empty(stream, wbytes, torch.uint8, x.device)
     elif work.numel() < wbytes:
         raise ValueError(f"workspace needs {wbytes} bytes")
     _check(lib().q4_gemm_packed(M, K, N, bs, _fmt(fmt), bits, _xdtype(x), _ptr(x), _ptr(packed), _ptr(y),
@@ -263,12 +263,12 @@ def gemm_packed(fmt: str, bs: int, x, packed, N: int, y=None, work=None, bits: i
     return y, (xq, xs, xsum)
 
 
-def _backward_work(M: int, K: int, N: int, work, device):
+def _backward_work(M: int, K: int, N: int, work, device, stream):
     nbytes = int(lib().q4_backward_work_bytes(M, K, N))
     if nbytes == 0:
         raise ValueError("invalid shape for the input gradient (K must be a multiple of 256)")
     if work is None:
-        return torch.empty(nbytes // 4, dtype=torch.float32, device=device)
+        return _empty(stream, nbytes // 4, torch.float32, device)
     if work.numel() * work.element_size() < nbytes:
         raise ValueError(f"workspace needs {nbytes} bytes")
     return work
@@ -278,8 +278,8 @@ def q4k_gemm_backward(blocks, dy, K: int, dx=None, work=None, stream=None):
     """Input gradient with frozen Q4_K weights: dy [M][N] -> dx [M][K] = dy . dequant(W)."""
     M, N = dy.shape
     if dx is None:
-        dx = torch.empty((M, K), dtype=torch.float32, device=dy.device)
-    work = _backward_work(M, K, N, work, dy.device)
+        dx = _empty(stream, (M, K), torch.float32, dy.device)
+    work = _backward_work(M, K, N, work, dy.device, stream)
     _check(lib().q4k_gemm_backward(M, K, N, _ptr(blocks), _ptr(dy), _ptr(dx), _ptr(work), _stream(stream)),
            "q4k_gemm_backward")
     return dx
@@ -299,8 +299,8 @@ def gemm_backward(fmt: str, bs: int, wq, wscale, wbias, dy, dx=None, work=None, 
     M, N = dy.shape
     K = 2 * wq.shape[1]
     if dx is None:
-        dx = torch.empty((M, K), dtype=torch.float32, device=dy.device)
-    work = _backward_work(M, K, N, work, dy.device)
+        dx = _empty(stream, (M, K), torch.float32, dy.device)
+    work = _backward_work(M, K, N, work, dy.device, stream)
     _check(lib().q4_gemm_backward(M, K, N, bs, _fmt(fmt), bits, _ptr(wq), _ptr(wscale), _ptr(wbias), _ptr(dy),
                                   _ptr(dx), _ptr(work), _stream(stream)), "q4_gemm_backward")
     return dx
@@ -309,7 +309,7 @@ def gemm_backward(fmt: str, bs: int, wq, wscale, wbias, dy, dx=None, work=None, 
 def q4k_gemv(blocks, x, N: int, y=None, stream=None):
     M, K = x.shape
     if y is None:
-        y = torch.empty((M, N), dtype=torch.float32, device=x.device)
+        y = _empty(stream, (M, N), torch.float32, x.device)
     _check(lib().q4k_gemv(M, K, N, _ptr(blocks), _ptr(x), _ptr(y), _stream(stream)), "q4k_gemv")
     return y
 
@@ -317,7 +317,7 @@ def q4k_gemv(blocks, x, N: int, y=None, stream=None):
 def q4k_gemm(blocks, x, N: int, y=None, stream=None):
     M, K = x.shape
     if y is None:
-        y = torch.empty((M, N), dtype=torch.float32, device=x.device)
+        y = _empty(stream, (M, N), torch.float32, x.device)
     _check(lib().q4k_gemm(M, K, N, _ptr(blocks), _ptr(x), _ptr(y), _stream(stream)), "q4k_gemm")
     return y
 
@@ -329,9 +329,9 @@ def q4k_gemm_work(blocks, x, N: int, y=None, work=None, stream=None):
     if nbytes == 0:
         raise ValueError("invalid shape for the Q4_K GEMM (K must be a multiple of 256)")
     if y is None:
-        y = torch.empty((M, N), dtype=torch.float32, device=x.device)
+        y = _empty(stream, (M, N), torch.float32, x.device)
     if work is None:
-        work = torch.empty(nbytes, dtype=torch.uint8, device=x.device)
+        work = _empty(stream, nbytes, torch.uint8, x.device)
     elif work.numel() * work.element_size() < nbytes:
         raise ValueError(f"workspace needs {nbytes} bytes")
     _check(lib().q4k_gemm_work(M, K, N, _ptr(blocks), _ptr(x), _ptr(y), _ptr(work), _stream(stream)),
@@ -344,11 +344,10 @@ def quantize_weights(w: torch.Tensor, fmt: str, bs: int, bits: int = 4, stream=N
     (affine) scales; affine codes may be 4, 6 or 8 bits wide."""
     N, K = w.shape
     f = _fmt(fmt)
-    wq = torch.empty(code_shape(N, K, bits) if bits in (4, 6, 8) else (N, K // 2), dtype=torch.uint8,
-                     device=w.device)
+    wq = _empty(stream, code_shape(N, K, bits) if bits in (4, 6, 8) else (N, K // 2), torch.uint8, w.device)
     sdt = torch.float16 if f == Q4_FMT_Q4_0 else torch.bfloat16
-    ws = torch.empty((N, K // bs), dtype=sdt, device=w.device)
-    wb = None if f == Q4_FMT_Q4_0 else torch.empty((N, K // bs), dtype=sdt, device=w.device)
+    ws = _empty(stream, (N, K // bs), sdt, w.device)
+    wb = None if f == Q4_FMT_Q4_0 else _empty(stream, (N, K // bs), sdt, w.device)
     _check(lib().q4_quantize_weights(N, K, bs, f, bits, _xdtype(w), _ptr(w), _ptr(wq), _ptr(ws), _ptr(wb),
                                      _stream(stream)), "q4_quantize_weights")
     return wq, ws, wb
@@ -357,7 +356,7 @@ def quantize_weights(w: torch.Tensor, fmt: str, bs: int, bits: int = 4, stream=N
 def q4k_quantize_weights(w: torch.Tensor, stream=None):
     """w [N][K] float32 -> Q4_K blocks uint8 [N][K/256*144]."""
     N, K = w.shape
-    blocks = torch.empty((N, K // 256 * Q4K_BLOCK_BYTES), dtype=torch.uint8, device=w.device)
+    blocks = _empty(stream, (N, K // 256 * Q4K_BLOCK_BYTES), torch.uint8, w.device)
     _check(lib().q4k_quantize_weights(N, K, _ptr(w), _ptr(blocks), _stream(stream)), "q4k_quantize_weights")
     return blocks
 

@@ -121,3 +121,34 @@ def test_streams_by_handle_and_under_a_context():
         assert stream_of_memory(y) == torch.cuda.default_stream().cuda_stream and torch.equal(y, want)
     with pytest.raises(AttributeError):
         q4.f8_linear(x, wq, ws, stream=7)
+
+
+def matmul_calls():
+    x = rand(30, 40, 512)
+    wq, wd, _ = q4.quantize_weights(rand(31, 256, 512), "q4_0", 32)
+    act, one = q4.quantize_act(x, 32), q4.quantize_act(x[:1], 32)
+    aq, ascale, abias = q4.quantize_weights(rand(32, 256, 512), "affine", 128)
+    packed = q4.pack_weights("affine", 128, aq, ascale, abias)
+    blocks, w, dy = q4.q4k_quantize_weights(rand(33, 256, 512)), rand(34, 256, 512), rand(35, 16, 256)
+    return {
+        "quantize_act": lambda **kw: q4.quantize_act(x, 32, **kw),
+        "gemv": lambda **kw: [q4.gemv("q4_0", 32, wq, wd, None, *one, **kw)],
+        "gemv_fused": lambda **kw: [q4.gemv_fused("q4_0", 32, x[:1], wq, wd, None, **kw)],
+        "gemm": lambda **kw: [q4.gemm("q4_0", 32, wq, wd, None, *act, **kw)],
+        "pack_weights": lambda **kw: [q4.pack_weights("affine", 128, aq, ascale, abias, **kw)],
+        "gemm_packed": lambda **kw: [q4.gemm_packed("affine", 128, x, packed, 256, **kw)[0]],
+        "q4k_gemv": lambda **kw: [q4.q4k_gemv(blocks, x[:1], 256, **kw)],
+        "q4k_gemm": lambda **kw: [q4.q4k_gemm(blocks, x, 256, **kw)],
+        "q4k_gemm_work": lambda **kw: [q4.q4k_gemm_work(blocks, x, 256, **kw)],
+        "q4k_gemm_backward": lambda **kw: [q4.q4k_gemm_backward(blocks, dy, 512, **kw)],
+        "gemm_backward": lambda **kw: [q4.gemm_backward("q4_0", 32, wq, wd, None, dy, **kw)],
+        "quantize_weights": lambda **kw: q4.quantize_weights(w, "q4_0", 32, **kw)[:2],
+        "q4k_quantize_weights": lambda **kw: [q4.q4k_quantize_weights(w, **kw)],
+    }
+
+
+@pytest.mark.parametrize("name", ["quantize_act", "gemv", "gemv_fused", "gemm", "pack_weights", "gemm_packed", "q4k_gemv",
+                                  "q4k_gemm", "q4k_gemm_work", "q4k_gemm_backward", "gemm_backward",
+                                  "quantize_weights", "q4k_quantize_weights"])
+def test_4_bit_products(name):
+    check(matmul_calls()[name])
