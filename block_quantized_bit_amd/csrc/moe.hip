@@ -680,6 +680,8 @@ __global__ __launch_bounds__(64 * DOWN_WAVES) void moe_down_kernel(Moe a) {
 // The same on the matrix cores, for affine experts with several tokens each:
 // sixteen rows a workgroup, one expert and half of k a wavefront.
 constexpr int MATRIX_WAVES = 16, HALVES = 2;
+constexpr size_t CU_LDS = 160 * 1024;
+static_assert((MOST_PAIRS + MATRIX_WAVES * 64) * 4 + HALVES * MOST_PAIRS * 16 * 4 <= CU_LDS, "lists and sums of any call");
 
 template <int G, bool YBF16>
 __global__ __launch_bounds__(64 * MATRIX_WAVES) void moe_down_matrix_kernel(Moe a, int stage) {
@@ -804,8 +806,11 @@ hipError_t launch(const Moe& a, hipStream_t stream) {
     if constexpr (FMT == 1)
         if (a.T * a.k >= 2 * slots) {  // two tokens an expert: what v_dot4 costs for two, the instruction costs for any
             auto kernel = moe_down_matrix_kernel<G, BF16>;
+            // scales and code sums are staged where they fit beside the sums (at most 128 KiB) and the lists of pairs;
+            // up to 48 KiB
             const size_t pairs = (size_t)a.T * a.k, sums = HALVES * pairs * 16 * 4, staged = pairs * (a.I / G) * 8;
-            const int stage = staged <= 48 * 1024;
+            const size_t lists = (MOST_PAIRS + MATRIX_WAVES * 64) * sizeof(int);
+            const int stage = staged <= 48 * 1024 && lists + sums + staged <= CU_LDS;
             const size_t bytes = sums + (stage ? staged : 0);
             e = bytes > 16384 ? ensure_dynamic_lds(reinterpret_cast<const void*>(kernel), bytes) : hipSuccess;
             if (e != hipSuccess) return e;

@@ -142,3 +142,16 @@ def test_refusals():
     many = torch.zeros(65, 128, device="cuda")
     with pytest.raises(q4.Q4Error):
         q4.moe_q4(many, torch.zeros(65, 4, device="cuda"), *weights, 2)
+
+
+@pytest.mark.parametrize("bs", [64, 128])
+@pytest.mark.parametrize("T,k,blocks", [(64, 16, 1), (64, 16, 3), (64, 16, 4), (64, 16, 6), (64, 16, 7), (56, 16, 6),
+                                        (53, 16, 7)])
+def test_many_pairs_fill_the_lds(T, k, blocks, bs):
+    """Up to 1024 pairs of token and expert, whose sums take 128 KiB: the hidden values' scales (8 bytes a pair and block)
+    are staged beside them only where both fit 160 KiB."""
+    print(f"case moe pairs T={T} k={k} blocks={blocks} {bs}", flush=True)
+    r = np.random.default_rng(T + blocks + bs)
+    weights, v13, v2 = layer(r, 20, 128, blocks * bs, "affine", bs)
+    x, logits = inputs(r, T, 128, 20, torch.float32)
+    check(x, logits, weights, v13, v2, k, "affine", bs)
