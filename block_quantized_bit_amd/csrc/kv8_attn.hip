@@ -17,18 +17,25 @@
 // long sequence is cut into splits, which a second launch joins: one sequence of
 // 1000 tokens 9.9 us, most of it launches and three dependent loads.
 //
-// Numbers. Codes are exact in f16. Queries are scaled per row by a power of
-// two into f16's range: bfloat16 queries are exact there (values more than
-// 2^22 below the row's largest are rounded), float32 ones are split into two
+// Numbers. Codes are exact in f16 and bfloat16. Queries are scaled per row by a
+// power of two into f16's range: bfloat16 queries are exact there (values more
+// than 2^22 below the row's largest are rounded), float32 ones are split into two
 // f16 halves. Products accumulate in float32. The page scales enter in float32:
-// the key scale multiplies the scores, the value scale vs the probabilities,
-// which go into the second product as f16. Their running reference is
-//     m = max_t (s_t + max(log2 vs_t, -80)),
-// not the largest score alone: p_t = 2^(s_t - m) then stays below 2^88 and the
-// weight p_t vs_t below 2^8 (move_reference lets m lag by that much), whatever the
-// scales of other pages are, and both sums (of p_t, and of p_t vs_t v_t) are in
-// units of 2^m. For bfloat16 results a weight is one f16 (2^-11 of itself, against
-// 2^-8 of the result's rounding), for float32 ones two halves.
+// the key scale multiplies the scores, the value scale vs the probabilities, which
+// are the weights of the second product. Their running reference is
+//     m = max_t (s_t + max(log2 vs_t, -80)) - LOW,
+// not the largest score alone: p_t = 2^(s_t - m) and the weight p_t vs_t are then
+// bounded whatever the scales of other pages are, and both sums (of p_t, and of
+// p_t vs_t v_t) are in units of 2^m.
+// For bfloat16 results a weight is one f16: 2^-12 of itself, against 2^-9 of the
+// result's rounding. LOW = 11 and a reference that lags by at most 2^4 hold the
+// largest weight between 2^11 and 2^15, so that weights keep their eleven bits down
+// to 2^-25 of it, and what is lost below is 2^-36 of it: where one token of small
+// value takes nearly all of the weight, the result is the other tokens'. (p_t stays
+// below 2^95, and a sum over 2^30 tokens finite.)
+// For float32 results a weight is three bfloat16 pieces (eight bits each, cut, not
+// rounded), which hold a float32 exactly at any size; there LOW = 0 and the
+// reference may lag by 2^8.
 #include <type_traits>
 
 #include "kernels_wide.h"
@@ -40,6 +47,8 @@ namespace {
 
 constexpr float NEG = -__builtin_inff();
 constexpr int CHUNK = 64;
+
+typedef __bf16 b8 __attribute__((ext_vector_type(8)));
 
 // 8 codes -> 8 f16, exactly. int8: the byte + 128 under 0x64 is the f16 value
 // 1024 + 128 + code.
@@ -61,6 +70,76 @@ __device__ __forceinline__ h8 codes_f16(uint32_t lo, uint32_t hi) {
     const h2 d = __builtin_bit_cast(h2, __builtin_amdgcn_perm(0x64646464u, hi, 0x04030402u)) + bias;
     return h8{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
 }
+
+// The upper 16 bits of two float32 values: bfloat16, the rest cut off.
+__device__ __forceinline__ uint32_t upper_halves(float lo, float hi) {
+    return __builtin_amdgcn_perm(__float_as_uint(hi), __float_as_uint(lo), 0x07060302u);
+}
+
+// 8 codes -> 8 bfloat16, exactly (seven and four bits).
+template <int FMT>
+__device__ __forceinline__ b8 codes_bf16(uint32_t lo, uint32_t hi) {
+    uint32_t w[4];
+    if (FMT == KV8_E4M3) {
+        w[0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 1.0f, false));
+        w[1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 1.0f, true));
+        w[2] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 1.0f, false));
+        w[3] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 1.0f, true));
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t c = (i < 2 ? lo : hi) >> (16 * (i & 1));
+            w[i] = upper_halves((float)(int8_t)(c & 0xFFu), (float)(int8_t)(c >> 8 & 0xFFu));
+        }
+    }
+    return __builtin_bit_cast(b8, make_uint4(w[0], w[1], w[2], w[3]));
+}
+
+// The operands of the second product: f16, and one piece a weight, for bfloat16
+// results; bfloat16, and three pieces a weight, for float32 ones.
+template <bool WIDE>
+struct Second;
+template <>
+struct Second<false> {
+    static constexpr int PIECES = 1;
+    static constexpr float LOW = 11.0f, LAG = 4.0f;  // see the head of the file
+    typedef h8 Op;
+    template <int FMT>
+    static __device__ __forceinline__ Op values(uint32_t lo, uint32_t hi) { return codes_f16<FMT>(lo, hi); }
+    static __device__ __forceinline__ void weights(const float (&w)[8], Op (&p)[PIECES]) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) p[0][i] = (_Float16)w[i];
+    }
+    static __device__ __forceinline__ v4f product(Op v, Op p, v4f c) {
+        return __builtin_amdgcn_mfma_f32_16x16x32_f16(v, p, c, 0, 0, 0);
+    }
+};
+template <>
+struct Second<true> {
+    static constexpr int PIECES = 3;
+    static constexpr float LOW = 0.0f, LAG = 8.0f;
+    typedef b8 Op;
+    template <int FMT>
+    static __device__ __forceinline__ Op values(uint32_t lo, uint32_t hi) { return codes_bf16<FMT>(lo, hi); }
+    static __device__ __forceinline__ void weights(const float (&w)[8], Op (&p)[PIECES]) {
+        float left[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) left[i] = w[i];
+#pragma unroll
+        for (int q = 0; q < PIECES; ++q) {
+            uint32_t x[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) x[i] = upper_halves(left[2 * i], left[2 * i + 1]);
+            p[q] = __builtin_bit_cast(Op, make_uint4(x[0], x[1], x[2], x[3]));
+            if (q + 1 < PIECES)
+#pragma unroll
+                for (int i = 0; i < 8; ++i) left[i] -= __uint_as_float(__float_as_uint(left[i]) & 0xFFFF0000u);  // exact
+        }
+    }
+    static __device__ __forceinline__ v4f product(Op v, Op p, v4f c) {
+        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(v, p, c, 0, 0, 0);
+    }
+};
 
 struct Attend {
     int total, max_new, max_kv, heads, group;  // group = heads / Hkv
@@ -135,12 +214,13 @@ __device__ __forceinline__ float column_max(float v) {
     return fmaxf(__uint_as_float(b0), __uint_as_float(b1));
 }
 
-// Moves a column's running reference m up to `top` and its sums with it, but only
-// once some column of the wavefront is more than 2^8 behind: until then weights
-// stay below 2^8, well inside f16, and most chunks leave the sums alone.
-template <int DT>
+// Moves a column's running reference m up to `top` - LOW and its sums with it, but
+// only once some column of the wavefront is more than 2^LAG behind: most chunks
+// leave the sums alone.
+template <bool WIDE, int DT>
 __device__ __forceinline__ void move_reference(float& m, float top, float& l, v4f (&o)[DT]) {
-    if (!__any(top > m + 8.0f)) return;
+    top -= Second<WIDE>::LOW;
+    if (!__any(top > m + Second<WIDE>::LAG)) return;
     const float to = fmaxf(m, top);
     const float f = __builtin_amdgcn_exp2f(m - (to == NEG ? 0.0f : to));
     m = to;
@@ -152,7 +232,7 @@ __device__ __forceinline__ void move_reference(float& m, float top, float& l, v4
 }
 
 // FMT: format of the codes; D: head size; RT: row tiles of 16; WIDE: float32
-// queries and results (two f16 halves each). The W wavefronts of a workgroup
+// queries (two f16 halves) and results. The W wavefronts of a workgroup
 // share its rows and take every W-th chunk. (Eight wavefronts without splits, one
 // launch instead of two, were no faster for one sequence of 1000 tokens, 12.0
 // against 11.0 us: a CU alone does not draw its 256 KB fast enough.)
@@ -163,6 +243,7 @@ __global__ __launch_bounds__(256) void kv8_attn_kernel(Kv8 c, Attend a) {
     constexpr int KL = D / 64;         // 16-byte loads of a lane's part of a key
     constexpr int W = 4;
     constexpr int HALVES = WIDE ? 2 : 1;
+    using S2 = Second<WIDE>;
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int r = lane & 15, g = lane >> 4;
@@ -297,7 +378,7 @@ __global__ __launch_bounds__(256) void kv8_attn_kernel(Kv8 c, Attend a) {
         }
 
         const float lv = fmaxf(__builtin_amdgcn_logf(vs), -80.0f);
-        h8 pf[RT][2][HALVES];
+        typename S2::Op pf[RT][2][S2::PIECES];
 #pragma unroll
         for (int u = 0; u < RT; ++u) {
             float top = NEG;
@@ -306,36 +387,33 @@ __global__ __launch_bounds__(256) void kv8_attn_kernel(Kv8 c, Attend a) {
 #pragma unroll
                 for (int e = 0; e < 4; ++e) top = fmaxf(top, st[u][t][e]);
             top = column_max(top + lv);
-            move_reference<DT>(m[u], top, l[u], o[u]);
+            move_reference<WIDE>(m[u], top, l[u], o[u]);
             const float ref = m[u] == NEG ? 0.0f : m[u];
             float sum = 0.0f;
 #pragma unroll
-            for (int t = 0; t < 4; ++t)
+            for (int half = 0; half < 2; ++half) {
+                float w[8];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const float p = __builtin_amdgcn_exp2f(st[u][t][e] - ref);
+                for (int j = 0; j < 8; ++j) {
+                    const float p = __builtin_amdgcn_exp2f(st[u][2 * half + j / 4][j % 4] - ref);
                     sum += p;
-                    float w = p * vs;
-                    // kept a float32 value of its own: folded into the conversion below, the product
-                    // would round to another f16 there than in the difference that gives the second half
-                    if (WIDE) __asm__("" : "+v"(w));
-                    const _Float16 hi = (_Float16)w;
-                    pf[u][t / 2][0][4 * (t & 1) + e] = hi;
-                    if (WIDE) pf[u][t / 2][HALVES - 1][4 * (t & 1) + e] = (_Float16)(w - (float)hi);
+                    w[j] = p * vs;
                 }
+                S2::weights(w, pf[u][half]);
+            }
             l[u] += sum;
         }
 
         // O^T
 #pragma unroll
         for (int d = 0; d < DT; ++d) {
-            const h8 v0 = codes_f16<FMT>(vc[d].x, vc[d].y), v1 = codes_f16<FMT>(vc[d].z, vc[d].w);
+            const auto v0 = S2::template values<FMT>(vc[d].x, vc[d].y), v1 = S2::template values<FMT>(vc[d].z, vc[d].w);
 #pragma unroll
             for (int u = 0; u < RT; ++u)
 #pragma unroll
-                for (int q = 0; q < HALVES; ++q) {
-                    o[u][d] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v0, pf[u][0][q], o[u][d], 0, 0, 0);
-                    o[u][d] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v1, pf[u][1][q], o[u][d], 0, 0, 0);
+                for (int q = 0; q < S2::PIECES; ++q) {
+                    o[u][d] = S2::product(v0, pf[u][0][q], o[u][d]);
+                    o[u][d] = S2::product(v1, pf[u][1][q], o[u][d]);
                 }
         }
     }
@@ -445,6 +523,7 @@ template <int FMT, int D, int RT, bool WIDE>
 __global__ __launch_bounds__(256, D == 64 || (D == 128 && !WIDE) ? 2 : 1) void kv8_many_kernel(Kv8 c, Attend a) {
     constexpr int KS = D / 32, DT = D / 16;
     constexpr int HALVES = WIDE ? 2 : 1;
+    using S2 = Second<WIDE>;
     constexpr int KP = D / 16;              // 16-code pieces of a key
     constexpr int LK = CHUNK * KP / 256;    // pieces a thread loads of K, and of V
     constexpr int ROWS = 64 * RT;
@@ -571,7 +650,7 @@ __global__ __launch_bounds__(256, D == 64 || (D == 128 && !WIDE) ? 2 : 1) void k
         vs_next = has_next ? c.v_scale[sat] : 0.0f;
     };
     auto key_of = [&](int tk) { return ((tk >> 4) << 2) | (tk & 3); };
-    auto store_f16 = [&](int buf) {
+    auto store_chunk = [&](int buf) {
         uint8_t* kl = lds + buf * L::STAGE;
         uint8_t* vl = kl + L::K;
 #pragma unroll
@@ -583,8 +662,9 @@ __global__ __launch_bounds__(256, D == 64 || (D == 128 && !WIDE) ? 2 : 1) void k
             *reinterpret_cast<h8*>(kl + tk * (2 * D) + 16 * ((2 * pc + 1) ^ key)) = codes_f16<FMT>(kraw[i].z, kraw[i].w);
             const int d = at >> 2, grp = at & 3;
             const int vkey = (d >> 1) & 7;
-            *reinterpret_cast<h8*>(vl + d * 128 + 16 * (grp ^ vkey)) = codes_f16<FMT>(vraw[i].x, vraw[i].y);
-            *reinterpret_cast<h8*>(vl + d * 128 + 16 * ((grp + 4) ^ vkey)) = codes_f16<FMT>(vraw[i].z, vraw[i].w);
+            using Op = typename S2::Op;
+            *reinterpret_cast<Op*>(vl + d * 128 + 16 * (grp ^ vkey)) = S2::template values<FMT>(vraw[i].x, vraw[i].y);
+            *reinterpret_cast<Op*>(vl + d * 128 + 16 * ((grp + 4) ^ vkey)) = S2::template values<FMT>(vraw[i].z, vraw[i].w);
         }
     };
 
@@ -593,7 +673,7 @@ __global__ __launch_bounds__(256, D == 64 || (D == 128 && !WIDE) ? 2 : 1) void k
         take_pages(from);
         load_raw(from);
         ask_pages(from + 1);
-        store_f16(0);
+        store_chunk(0);
     }
     for (int ch = from; ch < to; ++ch) {
         const int buf = (ch - from) & 1;
@@ -655,7 +735,7 @@ __global__ __launch_bounds__(256, D == 64 || (D == 128 && !WIDE) ? 2 : 1) void k
                 for (int t = 0; t < 4; ++t)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) top = fmaxf(top, st[u][t][e]);
-                move_reference<DT>(m[u], column_max(fmaf(top, fac[u], lv)), l[u], o[u]);
+                move_reference<WIDE>(m[u], column_max(fmaf(top, fac[u], lv)), l[u], o[u]);
                 const float ref = m[u] == NEG ? 0.0f : m[u];
                 // for bfloat16 results the value scale enters through the exponent (its logarithm is good to
                 // 2^-21), and the plain sum takes it out again
@@ -665,38 +745,30 @@ __global__ __launch_bounds__(256, D == 64 || (D == 128 && !WIDE) ? 2 : 1) void k
             // exponentials of the second
 #pragma unroll
             for (int w = 0; w < 2; ++w) {
-                h8 pf[RT][HALVES];
+                typename S2::Op pf[RT][S2::PIECES];
 #pragma unroll
                 for (int u = 0; u < RT; ++u) {
-                    float sum = 0.0f;
+                    float sum = 0.0f, x[8];
 #pragma unroll
                     for (int j = 0; j < 8; ++j) {
                         const float p = __builtin_amdgcn_exp2f(fmaf(st[u][2 * w + j / 4][j % 4], fac[u], less[u]));
                         sum += p;
-                        if (WIDE) {
-                            float x = p * vs;
-                            __asm__("" : "+v"(x));  // a float32 value of its own, as in the kernel above
-                            const _Float16 hi = (_Float16)x;
-                            pf[u][0][j] = hi;
-                            pf[u][HALVES - 1][j] = (_Float16)(x - (float)hi);
-                        } else {
-                            pf[u][0][j] = (_Float16)p;
-                        }
+                        x[j] = WIDE ? p * vs : p;
                     }
+                    S2::weights(x, pf[u]);
                     l[u] = fmaf(sum, unit, l[u]);
                 }
 #pragma unroll
                 for (int d = 0; d < DT; ++d) {
-                    const h8 v = *reinterpret_cast<const h8*>(vl + (16 * d + r) * 128 + 16 * ((g + 4 * w) ^ (r >> 1)));
+                    const auto v = *reinterpret_cast<const typename S2::Op*>(vl + (16 * d + r) * 128 + 16 * ((g + 4 * w) ^ (r >> 1)));
 #pragma unroll
                     for (int u = 0; u < RT; ++u)
 #pragma unroll
-                        for (int q = 0; q < HALVES; ++q)
-                            o[u][d] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v, pf[u][q], o[u][d], 0, 0, 0);
+                        for (int q = 0; q < S2::PIECES; ++q) o[u][d] = S2::product(v, pf[u][q], o[u][d]);
                 }
             }
         }
-        if (ch + 1 < to) store_f16(buf ^ 1);
+        if (ch + 1 < to) store_chunk(buf ^ 1);
     }
 
 #pragma unroll
