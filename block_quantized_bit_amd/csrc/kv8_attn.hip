@@ -508,7 +508,7 @@ __global__ __launch_bounds__(256) void kv8_attn_kernel(Kv8 c, Attend a) {
 // the key of a token is its row in the first product and that of a value row half
 // its number, so that the sixteen lanes that a 16-byte read serves at once, which
 // come from two lane groups, fall on different banks.
-// Two chunks of 1024 tokens, 32 heads over 8, up to 4096 keys: 146 us, 0.6
+// Two chunks of 1024 tokens, 32 heads over 8, up to 4096 keys: 148 us, 0.6
 // PFLOP/s. Counters: VALU 32%, matrix cores 21% of the time, the two wavefronts of
 // a SIMD (244 registers each) wait for each other and for LDS in the rest.
 // Scores stay unscaled in their registers: the factor ks * qs is the same for
@@ -723,8 +723,10 @@ __global__ __launch_bounds__(256, D == 64 || (D == 128 && !WIDE) ? 2 : 1) void k
                             st[u][t][e] = see ? st[u][t][e] : NEG;
                         }
             }
-            const float lv = fmaxf(__builtin_amdgcn_logf(vs), -80.0f);
-            const float unit = WIDE ? 1.0f : __builtin_amdgcn_exp2f(-lv);
+            const float lvs = __builtin_amdgcn_logf(vs), lv = fmaxf(lvs, -80.0f);
+            // for bfloat16 results the value scale enters through the exponent (its logarithm is good to 2^-21, against
+            // the weights' 2^-12), and the plain sum takes it out again
+            float unit = WIDE ? 1.0f : __builtin_amdgcn_exp2f(-lv);
             float fac[RT], less[RT];
 #pragma unroll
             for (int u = 0; u < RT; ++u) {
@@ -737,9 +739,22 @@ __global__ __launch_bounds__(256, D == 64 || (D == 128 && !WIDE) ? 2 : 1) void k
                     for (int e = 0; e < 4; ++e) top = fmaxf(top, st[u][t][e]);
                 move_reference<WIDE>(m[u], column_max(fmaf(top, fac[u], lv)), l[u], o[u]);
                 const float ref = m[u] == NEG ? 0.0f : m[u];
-                // for bfloat16 results the value scale enters through the exponent (its logarithm is good to
-                // 2^-21), and the plain sum takes it out again
-                less[u] = WIDE ? -ref : lv - ref;
+                less[u] = WIDE ? -ref : lvs - ref;
+            }
+            // below 2^-80 (and without a page) a score's part of the plain sum cannot be had from its weight: summed
+            // by itself (148 us for the two chunks of 1024; a factor on every weight instead 151)
+            if (!WIDE && __any(lvs < lv)) {
+#pragma unroll
+                for (int u = 0; u < RT; ++u) {
+                    const float ref = m[u] == NEG ? 0.0f : m[u];
+                    float sum = 0.0f;
+#pragma unroll
+                    for (int t = 0; t < 4; ++t)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) sum += __builtin_amdgcn_exp2f(fmaf(st[u][t][e], fac[u], -ref));
+                    l[u] += lvs < lv ? sum : 0.0f;
+                }
+                unit = lvs < lv ? 0.0f : unit;
             }
             // half of the tokens at a time: the products of the first half's weights run under the
             // exponentials of the second

@@ -85,6 +85,7 @@ size_t kv8_attention_work_bytes(const kv8_cache* cache, int total, int max_new, 
  * Softmax statistics and sums are float32, and codes enter the products exactly. For float32 results queries enter as
  * two f16 halves (22 bits of the row's largest value) and weights p_t in full. For bfloat16 results queries are exact
  * (22 bits of the row's largest value) and a weight is rounded to f16's eleven bits, or to 2^-36 of the largest one.
+ * (Where all value scales lie below 2^-80, say at 2^(-80 - k), that is 2^(k - 36) of the largest one.)
  */
 int kv8_attention(const kv8_cache* cache, int total, int max_new, int max_kv, int heads, int dtype, const void* q,
                   long long q_stride, float scale, int window, void* out, float* lse, void* work, void* stream);

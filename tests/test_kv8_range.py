@@ -1,5 +1,5 @@
-"""Attention over the 8-bit cache where weights lie many powers of two below the largest, in the kernels for few and for
-many rows, against 64-bit values on the CPU."""
+"""Attention over the 8-bit cache where weights lie many powers of two below the largest, and with value scales from
+2^-100 up, in the kernels for few and for many rows, against 64-bit values on the CPU."""
 import numpy as np
 import pytest
 import torch
@@ -85,3 +85,17 @@ def test_a_token_of_no_value_takes_most_of_the_weight(share, n, dtype, kind):
         others = s.max(1) + np.log(np.exp(s - s.max(1, keepdims=True)).sum(1))
         q[i, :, 0] = (others + np.log(share / (1 - share))) / (scale * k[0, 0])
     check(torch.from_numpy(q.astype(np.float32)).cuda().to(dtype), cache, table, L, dtype, scale)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("n", [1, 100])
+@pytest.mark.parametrize("low,high", [(-100, -84), (-100, 20), (-40, 20)])
+def test_value_scales_of_any_size(low, high, n, dtype):
+    print(f"case scales 2^{low} .. 2^{high} n={n} {dtype}", flush=True)
+    r = np.random.default_rng(n - low)
+    cache, table = random_cache(r, 200, 16, 64, torch.int8)
+    cache.scale[1] = 2.0 ** r.integers(low, high, cache.scale[1].shape)
+    cache.scale[1, table[3]] = 0.0
+    cache.codes[1, table[3]] = 0.0
+    q = torch.from_numpy(r.standard_normal((n, 4, 64)).astype(np.float32)).cuda().to(dtype)
+    check(q, cache, table, 200, dtype, 0.125)
