@@ -156,6 +156,12 @@ struct Attend {
 };
 
 constexpr float LN2 = 0.6931471805599453f;
+
+// Logarithm of a row's sum l 2^m: -infinity only for a row that sees no key (a NaN query has no maximum either, but
+// its sum is NaN).
+__device__ __forceinline__ float log_of_sum(float m, float l) {
+    return l == 0.0f ? NEG : (m + __builtin_amdgcn_logf(l)) * LN2;
+}
 // Rows of a sequence and head that the first kernel takes: 40 rows over a window of 512 keys took it 12 us, the
 // kernel for many rows 18 us.
 constexpr int FEW_ROWS = 64;
@@ -492,7 +498,7 @@ __global__ __launch_bounds__(256) void kv8_attn_kernel(Kv8 c, Attend a) {
                 if (a.splits > 1)
                     a.part_ml[(long long)split * a.total * a.heads + orow[u]] = make_float2(m[u], l[u]);
                 else if (a.lse)
-                    a.lse[orow[u]] = m[u] == NEG ? NEG : (m[u] + __builtin_amdgcn_logf(l[u])) * LN2;
+                    a.lse[orow[u]] = log_of_sum(m[u], l[u]);
             }
 }
 
@@ -808,7 +814,7 @@ __global__ __launch_bounds__(256, D == 64 || (D == 128 && !WIDE) ? 2 : 1) void k
             if (a.splits > 1)
                 a.part_ml[(long long)split * a.total * a.heads + orow[u]] = make_float2(m[u], l[u]);
             else if (a.lse)
-                a.lse[orow[u]] = m[u] == NEG ? NEG : (m[u] + __builtin_amdgcn_logf(l[u])) * LN2;
+                a.lse[orow[u]] = log_of_sum(m[u], l[u]);
         }
     }
 }
@@ -845,7 +851,7 @@ __global__ __launch_bounds__(256) void kv8_join_kernel(Attend a) {
             else
                 static_cast<uint16_t*>(a.out)[row * D + E * lane + e] = (uint16_t)bf16_bits(v[e] * inv);
         }
-        if (a.lse && lane == 0) a.lse[row] = top == NEG ? NEG : (top + __builtin_amdgcn_logf(l)) * LN2;
+        if (a.lse && lane == 0) a.lse[row] = log_of_sum(top, l);
     }
 }
 

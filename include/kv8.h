@@ -81,7 +81,7 @@ size_t kv8_attention_work_bytes(const kv8_cache* cache, int total, int max_new, 
  *   out[r][h] = sum_t p_t v_t,  p = softmax_t(scale * q . k_t)
  * over the positions t <= that of the query, with window > 0 only the last `window` of them, and t < max_kv. A query
  * that sees no key gives zeros. out [total][heads][D] in q's dtype, contiguous. lse [total][heads] float32 may be
- * NULL: log(sum_t exp(scale * q . k_t)), -infinity for a query that sees no key.
+ * NULL: log(sum_t exp(scale * q . k_t)), -infinity for a query that sees no key. A query with a NaN gives NaN in both.
  * Softmax statistics and sums are float32, and codes enter the products exactly. For float32 results queries enter as
  * two f16 halves (22 bits of the row's largest value) and weights p_t in full. For bfloat16 results queries are exact
  * (22 bits of the row's largest value) and a weight is rounded to f16's eleven bits, or to 2^-36 of the largest one.

@@ -99,3 +99,28 @@ def test_value_scales_of_any_size(low, high, n, dtype):
     cache.codes[1, table[3]] = 0.0
     q = torch.from_numpy(r.standard_normal((n, 4, 64)).astype(np.float32)).cuda().to(dtype)
     check(q, cache, table, 200, dtype, 0.125)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("n,L", [(1, 40), (1, 3000), (100, 150), (100, 3000)])
+def test_a_query_with_a_nan(n, L, dtype):
+    """One head's last query holds a NaN: its result and its lse are NaN (not those of a query that sees no key), every
+    other one is as it was. Few and many rows, in one part and in splits."""
+    print(f"case NaN query n={n} L={L} {dtype}", flush=True)
+    r = np.random.default_rng(n + L)
+    cache, table = random_cache(r, L, 64, 64, torch.int8)
+    q = torch.from_numpy(r.standard_normal((n, 4, 64)).astype(np.float32)).cuda().to(dtype)
+    q[-1, 2, 7] = float("nan")
+    lse = torch.zeros(n, 4, device="cuda")
+    out = q4.kv8_attention(q, *cache.tensors(), i32(table[None].tolist()), i32([L]), i32([0, n]), n, L, lse=lse)
+    assert out[-1, 2].isnan().all() and lse[-1, 2].isnan()
+    k, v = (cache.values(w, table, 0, L) for w in range(2))
+    qf = W.as_f64(q)
+    qf[-1, 2] = 0.0
+    want, wlse, mass = W.attention(qf, k, v, L - n + np.arange(n), 0.125, 0)
+    spread = 0.125 * max((np.abs(qf[:, h]) @ np.abs(k[:, 0]).T).max() for h in range(4))
+    good = np.ones((n, 4), dtype=bool)
+    good[-1, 2] = False
+    flush = L * 2.0 ** -36 * 127 * cache.scale[1].max()
+    assert (np.abs(W.as_f64(out) - want) <= bound(mass, L, spread, flush, dtype))[good].all()
+    assert (np.abs(W.as_f64(lse) - wlse)[good] <= 4 * 2.0 ** -20 * (spread + 1) + (L / 16 + 64) * 2.0 ** -24).all()
