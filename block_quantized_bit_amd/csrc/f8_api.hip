@@ -87,10 +87,11 @@ size_t f8_linear_work_bytes(int M, int K) {
 
 int f8_linear(int M, int K, int N, int xdtype, const void* x, long long x_stride, const uint8_t* wq, const float* ws,
               void* y, void* work, void* stream) {
-    if (!x || !wq || !ws || !y || !work) return Q4_ERR_NULL;
+    if (!x || !wq || !ws || !y) return Q4_ERR_NULL;
     const int st = check_x(M, K, xdtype, x, x_stride);
     if (st) return st;
     if (!size_ok(N, K) || !product_ok(M, N)) return Q4_ERR_DIM;
+    if (!work) return Q4_ERR_NULL;  // after the sizes: those that are refused have a workspace of 0 bytes
     if (!aligned(wq, 16) || !aligned(ws, 4) || !aligned(y, 16) || !aligned(work, 16)) return Q4_ERR_ALIGN;
     const hipStream_t s = static_cast<hipStream_t>(stream);
     const bool bf16 = xdtype == Q4_DT_BF16;
@@ -115,12 +116,13 @@ size_t f8_linear_backward_work_bytes(int M, int K, int N) {
 int f8_linear_backward(int M, int K, int N, int dtype, const void* dy, long long dy_stride, const void* x,
                        long long x_stride, const uint8_t* wqt, const float* wst, void* dx, int dwtype, void* dw,
                        void* work, void* stream) {
-    if (!dy || !work || (!dx && !dw) || (dx && (!wqt || !wst)) || (dw && !x)) return Q4_ERR_NULL;
+    if (!dy || (!dx && !dw) || (dx && (!wqt || !wst)) || (dw && !x)) return Q4_ERR_NULL;
     if (dw && !type_ok(dwtype)) return Q4_ERR_FORMAT;
     int st = check_x(M, N, dtype, dy, dy_stride);
     if (st) return st;
     if (dw && (st = check_x(M, K, dtype, x, x_stride))) return st;
     if (!f8_linear_backward_work_bytes(M, K, N)) return Q4_ERR_DIM;
+    if (!work) return Q4_ERR_NULL;
     if (!aligned(dx, 16) || !aligned(dw, 16) || !aligned(wqt, 16) || !aligned(wst, 4) || !aligned(work, 16))
         return Q4_ERR_ALIGN;
     const hipStream_t s = static_cast<hipStream_t>(stream);

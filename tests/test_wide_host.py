@@ -231,3 +231,16 @@ def test_a_planted_mistake_exceeds_the_bounds(mistake):
         got = want / np.arange(37, 41)[:, None, None]
     spread = 0.25 * max((np.abs(q[:, h]) @ np.abs(k[:, 0]).T).max() for h in range(2))
     assert (np.abs(got - want) > bound(mass, 40, spread, torch.bfloat16)).any()
+
+
+def test_sizes_are_refused_as_such_without_a_workspace():
+    """Sizes beyond the limits have no workspace (its size is 0, its pointer may be null): the status names the size."""
+    linear = func("f8_linear", I, I, I, I, P, LL, P, P, P, P, P)
+    back = func("f8_linear_backward", I, I, I, I, P, LL, P, LL, P, P, P, I, P, P, P)
+    big = 1 << 23
+    for M, K, N in ((big, 128, 8), (4, big, 8), (4, 128, big), (0, 128, 8)):
+        assert linear(M, K, N, 0, A, K, A, A, A, None, None) == DIM
+        assert back(M, K, N, 0, A, N, A, K, A, A, A, 0, A, None, None) == DIM
+    assert linear(1 << 21, 128, 1 << 21, 0, A, 128, A, A, A, None, None) == DIM  # outputs beyond the grid
+    assert back(4, 128, 8, 0, A, 8, A, 128, A, A, A, 0, A, None, None) == NULL
+    assert linear(4, 128, 8, 0, None, 128, A, A, A, None, None) == NULL
