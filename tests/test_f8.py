@@ -233,3 +233,32 @@ def test_refusals():
         q4.f8_linear(x[:0], wq, ws)
     with pytest.raises(ValueError):
         q4.f8_linear_backward(x, x[:2], wq, ws)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("K", [100, 300, 640, 1152])
+def test_linear_middle_tiles(K, dtype):
+    """288 tiles of 128 x 128 (fewer than 256 of 256 x 256), ragged on all sides: one block of k, and numbers of blocks
+    that are no multiple of the four stages."""
+    M, N = 1030, 3970
+    print(f"case linear middle tiles {M} {K} {N} {dtype}", flush=True)
+    x = activations(M, K, dtype)
+    wq, ws, c, s = weights(N, K)
+    y, a = W.f8_product(*W.f8_rows(W.as_f64(x)), c, s)
+    out = torch.full((M, N), float("nan"), dtype=dtype, device="cuda")
+    got = W.as_f64(q4.f8_linear(x, wq, ws, out=out))
+    assert (np.abs(got - y) <= W.f8_bound(a, (K + 127) // 128, y, dtype)).all()
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("M,K,N", [(70, 1030, 3970), (700, 1030, 3970), (300, 4100, 4100)])
+def test_weight_gradient_middle_and_large_tiles(M, K, N, dtype):
+    """288 tiles of 128 x 128, and for bfloat16 289 of 256 x 256, with scales per row on both sides; M gives one, three
+    and six blocks."""
+    print(f"case weight gradient tiles {M} {K} {N} {dtype}", flush=True)
+    x = activations(M, K, dtype)
+    dy = (0.01 * activations(M, N, torch.float32, 1)).to(dtype)
+    dw = torch.full((N, K), float("nan"), dtype=dtype, device="cuda")
+    q4.f8_linear_backward(dy, x, None, None, need_dx=False, dw=dw)
+    y, a = W.f8_product_rows(*W.f8_rows(W.as_f64(dy).T), *W.f8_rows(W.as_f64(x).T))
+    assert (np.abs(W.as_f64(dw) - y) <= W.f8_bound(a, (M + 127) // 128, y, dtype)).all()

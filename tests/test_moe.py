@@ -155,3 +155,29 @@ def test_many_pairs_fill_the_lds(T, k, blocks, bs):
     weights, v13, v2 = layer(r, 20, 128, blocks * bs, "affine", bs)
     x, logits = inputs(r, T, 128, 20, torch.float32)
     check(x, logits, weights, v13, v2, k, "affine", bs)
+
+
+@pytest.mark.parametrize("aligned", [True, False])
+@pytest.mark.parametrize("bs", [64, 128])
+@pytest.mark.parametrize("H,inter", [(512, 512), (1024, 1536), (512, 640), (640, 512)])
+def test_scales_of_four_steps_in_one_load(H, inter, bs, aligned):
+    """Rows of scales that start on 8 or 16 bytes come four steps at a time (H or I a multiple of 512, for each of the
+    two products by itself), others one by one: the same layer with scales at an odd offset."""
+    print(f"case moe wide scales {H} {inter} {bs} {aligned}", flush=True)
+    r = np.random.default_rng(H + inter + bs)
+    (w13, s13, b13, w2, s2, b2), v13, v2 = layer(r, 3, H, inter, "affine", bs)
+    if not aligned:
+        def moved(t):
+            return torch.cat([t.new_zeros(1), t.flatten()])[1:].view(t.shape)
+        s13, b13, s2, b2 = (moved(t) for t in (s13, b13, s2, b2))
+        assert s13.data_ptr() % 16 == 2 and s13.is_contiguous()
+    x, logits = inputs(r, 20, H, 3, torch.float32)
+    check(x, logits, (w13, s13, b13, w2, s2, b2), v13, v2, 2, "affine", bs)
+
+
+def test_scales_that_are_not_staged():
+    """128 pairs of 128 blocks: 128 KiB of scales and sums of the hidden values, read from memory."""
+    r = np.random.default_rng(7)
+    weights, v13, v2 = layer(r, 4, 128, 8192, "affine", 64)
+    x, logits = inputs(r, 64, 128, 4, torch.float32)
+    check(x, logits, weights, v13, v2, 2, "affine", 64)
