@@ -56,6 +56,12 @@ long integer(PyObject* o, const char* what) {
     return v;
 }
 
+bool truth(PyObject* o) {
+    const int v = PyObject_IsTrue(o);
+    if (v < 0) throw PythonProblem();
+    return v == 1;
+}
+
 const c10::impl::VirtualGuardImpl& gpu() {
     static const c10::impl::VirtualGuardImpl impl(c10::DeviceType::CUDA);
     return impl;
@@ -218,7 +224,7 @@ PyObject* linear_backward(PyObject*, PyObject* const* a, Py_ssize_t) {
         const c10::Device dev = device_of(dy, "dy");
         const OnStream on(a[9], dev);
         const Rows d = rows_of(dy, dev, "dy");
-        const bool need_dx = PyObject_IsTrue(a[6]) == 1, need_dw = PyObject_IsTrue(a[7]) == 1;
+        const bool need_dx = truth(a[6]), need_dw = truth(a[7]);
         const auto type = dy.scalar_type();
         Rows x{d.dtype, d.M, 0, 0, nullptr};
         if (need_dw || !none(a[1])) {
@@ -403,7 +409,7 @@ PyObject* moe(PyObject*, PyObject* const* a, Py_ssize_t) {
         const at::Tensor work =
             workspace(a[13], moe_q4_work_bytes((int)T, (int)H, (int)I, (int)E, top_k, bs), dev);
         check(moe_q4((int)T, (int)H, (int)I, (int)E, top_k, bs, fmt, dt, px, (const float*)pl, (const uint8_t*)p13, ps13,
-                     pb13, (const uint8_t*)p2, ps2, pb2, PyObject_IsTrue(a[11]) == 1, po, work.data_ptr(),
+                     pb13, (const uint8_t*)p2, ps2, pb2, truth(a[11]), po, work.data_ptr(),
                      on.handle),
               "moe_q4");
         return THPVariable_Wrap(out);

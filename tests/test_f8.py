@@ -262,3 +262,10 @@ def test_weight_gradient_middle_and_large_tiles(M, K, N, dtype):
     q4.f8_linear_backward(dy, x, None, None, need_dx=False, dw=dw)
     y, a = W.f8_product_rows(*W.f8_rows(W.as_f64(dy).T), *W.f8_rows(W.as_f64(x).T))
     assert (np.abs(W.as_f64(dw) - y) <= W.f8_bound(a, (M + 127) // 128, y, dtype)).all()
+
+
+def test_flags_without_a_truth_value():
+    """need_dx and need_dw are asked for their truth; an object that has none raises its own error."""
+    x, dy = activations(4, 128, torch.float32), activations(4, 64, torch.float32)
+    with pytest.raises(RuntimeError, match="[Bb]oolean"):
+        q4.f8_linear_backward(dy, x, None, None, need_dx=False, need_dw=torch.ones(2))
