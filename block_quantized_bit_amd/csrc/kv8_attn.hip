@@ -36,6 +36,7 @@
 // For float32 results a weight is three bfloat16 pieces (eight bits each, cut, not
 // rounded), which hold a float32 exactly at any size; there LOW = 0 and the
 // reference may lag by 2^8.
+#include <algorithm>
 #include <type_traits>
 
 #include "kernels_wide.h"
@@ -863,7 +864,7 @@ struct Plan {
 };
 
 // How a call is cut: from the sizes alone, so that the workspace is known
-// before the launch.
+// before the launch. (std::min: HIP's own min for the host takes two ints.)
 Plan plan_of(int B, int H, int D, int group, int max_new, int max_kv, int window) {
     Plan p;
     const long long rows = (long long)max_new * group;
@@ -873,16 +874,16 @@ Plan plan_of(int B, int H, int D, int group, int max_new, int max_kv, int window
     p.tiles = (int)((rows + tile - 1) / tile);
     // chunks that a row tile can see
     long long span = max_kv;
-    if (window > 0) span = min(span, (long long)window + tile / group + 1);
+    if (window > 0) span = std::min(span, (long long)window + tile / group + 1);
     const int chunks = (int)((span + CHUNK - 1) / CHUNK) + (window > 0 ? 1 : 0);
     const long long wgs = (long long)p.tiles * H * B;
     // enough workgroups for the chip (three a CU for the memory-bound kernel, two for the other), no split below
     // two chunks (few rows: one sequence of 1000 tokens took 11 us with two or four, 13 with one) or eight
     const int least = p.share ? 2 : 8;
-    const long long fill = min(p.share ? (768 + wgs - 1) / wgs : wgs < 256 ? (512 + wgs - 1) / wgs : 1LL, (long long)MOST_SPLITS);
-    const long long want = max(1LL, min(fill, (long long)(chunks + least - 1) / least));
+    const long long fill = std::min(p.share ? (768 + wgs - 1) / wgs : wgs < 256 ? (512 + wgs - 1) / wgs : 1LL, (long long)MOST_SPLITS);
+    const long long want = std::max(1LL, std::min(fill, (long long)(chunks + least - 1) / least));
     const long long all = (max_kv + CHUNK - 1) / CHUNK + 1;
-    p.most_splits = (int)max(1LL, min(fill, (all + least - 1) / least));
+    p.most_splits = (int)std::max(1LL, std::min(fill, (all + least - 1) / least));
     p.chunks_per_split = (int)((chunks + want - 1) / want);
     p.splits = (chunks + p.chunks_per_split - 1) / p.chunks_per_split;
     return p;
@@ -907,7 +908,7 @@ hipError_t launch_attn(const Kv8& c, const Attend& a, const Plan& p, hipStream_t
         go(kv8_attn_kernel<FMT, D, MOST, WIDE>, 0);
     if (e != hipSuccess || p.splits == 1) return e;
     const long long rows = (long long)a.total * a.heads;
-    hipLaunchKernelGGL((kv8_join_kernel<D, WIDE>), dim3((unsigned)min((rows + 3) / 4, 1LL << 20)), dim3(256), 0,
+    hipLaunchKernelGGL((kv8_join_kernel<D, WIDE>), dim3((unsigned)std::min((rows + 3) / 4, 1LL << 20)), dim3(256), 0,
                        stream, a);
     return hipGetLastError();
 }
@@ -925,6 +926,8 @@ size_t kv8_attn_work_bytes(const Kv8& c, int total, int max_new, int max_kv, int
 hipError_t launch_kv8_attention(const Kv8& c, int format, int total, int max_new, int max_kv, int heads, bool bf16,
                                 const void* q, long long q_stride, float scale, int window, void* out, float* lse,
                                 void* work, hipStream_t stream) {
+    // positions lie below 2^30, so a longer window hides nothing; the kernels subtract it from positions in 32 bits
+    if (window >= 1 << 30) window = 0;
     const Plan p = plan_of(c.B, c.H, c.D, heads / c.H, max_new, max_kv, window);
     Attend a;
     a.total = total;

@@ -124,3 +124,18 @@ def test_a_query_with_a_nan(n, L, dtype):
     flush = L * 2.0 ** -36 * 127 * cache.scale[1].max()
     assert (np.abs(W.as_f64(out) - want) <= bound(mass, L, spread, flush, dtype))[good].all()
     assert (np.abs(W.as_f64(lse) - wlse)[good] <= 4 * 2.0 ** -20 * (spread + 1) + (L / 16 + 64) * 2.0 ** -24).all()
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("window", [2 ** 31 - 1, 2 ** 30, 2 ** 30 - 1])
+@pytest.mark.parametrize("L,n", [(40, 1), (3, 6), (90, 100), (300, 100)])
+def test_a_window_as_long_as_an_int_can_say(L, n, window, dtype):
+    """Such a window hides nothing, also where queries stand before position 0 (more of them than the length)."""
+    print(f"case window {window} L={L} n={n} {dtype}", flush=True)
+    r = np.random.default_rng(L + n)
+    cache, table = random_cache(r, L, 16, 64, torch.int8)
+    q = torch.from_numpy(r.standard_normal((n, 4, 64)).astype(np.float32)).cuda().to(dtype)
+    args = (*cache.tensors(), i32(table[None].tolist()), i32([L]), i32([0, n]), n, L)
+    want = q4.kv8_attention(q, *args)
+    assert n > L or want.abs().amin() > 0
+    assert torch.equal(q4.kv8_attention(q, *args, window=window), want)
