@@ -379,13 +379,13 @@ __global__ __launch_bounds__(64 * Up<G>::WAVES) void moe_up_kernel(Moe a, int ba
             const int grp = at / L, k0 = grp * G + (at & (L - 1)) * EPT;
             const long long src = (long long)token(tk) * H + k0;
             float v[EPT];
-            float amax = 0.0f;
+            uint32_t top = 0;
 #pragma unroll
             for (int j = 0; j < EPT; ++j) {
                 v[j] = load_as_float<XBF16>(a.x, src + j);
-                amax = fmaxf(amax, fabsf(v[j]));
+                top = max(top, magnitude(v[j]));
             }
-            amax = row_max16(amax);
+            const float amax = __uint_as_float(row_max16(top));  // a NaN if there is one: it makes the scale NaN
             const float s = amax / 127.0f;
             const float inv = act_inverse(s);
             int q[EPT], sum = 0;
@@ -560,14 +560,14 @@ __global__ __launch_bounds__(64 * Up<G>::WAVES) void moe_up_kernel(Moe a, int ba
         for (int it = tid; it < n * L; it += NT) {
             const int tk = it / L, k0 = (it & (L - 1)) * EPT;
             float v[EPT];
-            float amax = 0.0f;
+            uint32_t top = 0;
 #pragma unroll
             for (int j = 0; j < EPT; ++j) {
                 const float g = hid[tk * G + k0 + j], u = hid[(batch + tk) * G + k0 + j];
                 v[j] = g / (1.0f + expf(-g)) * u;
-                amax = fmaxf(amax, fabsf(v[j]));
+                top = max(top, magnitude(v[j]));
             }
-            amax = row_max16(amax);
+            const float amax = __uint_as_float(row_max16(top));
             const float s = amax / 127.0f;
             const float inv = act_inverse(s);
             const int pair = mine[first + tk];

@@ -90,6 +90,16 @@ __device__ __forceinline__ float row_max16(float v) {
     return v;
 }
 
+// The same for unsigned integers: of magnitude() bits, which order as the values do with NaN above infinity.
+__device__ __forceinline__ uint32_t row_max16(uint32_t v) {
+    v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0xB1, 0xF, 0xF, false));
+    v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x4E, 0xF, 0xF, false));
+    v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x141, 0xF, 0xF, false));
+    v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x140, 0xF, 0xF, false));
+    return v;
+}
+__device__ __forceinline__ uint32_t magnitude(float v) { return __float_as_uint(v) & 0x7FFFFFFFu; }
+
 // ---- e4m3 -------------------------------------------------------------------
 
 constexpr float F8_TOP = 448.0f;

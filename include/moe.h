@@ -12,7 +12,8 @@
  *
  * The products are those of q4_gemv: x and h are quantized per block to int8
  * (q4_quantize_act), each block's dot is an exact integer, and the block's
- * scales (and the affine bias) are applied in float32.
+ * scales (and the affine bias) are applied in float32. Unlike there, a block
+ * with a NaN has a NaN scale: a token with a NaN or an infinity gives NaN.
  *
  * Layouts (codes, scales and formats of q4.h, bits = 4):
  *   w13 [E][2 I][H/2] codes: rows 0 .. I-1 of an expert are W1 (gate), rows I .. 2I-1 W3 (up);

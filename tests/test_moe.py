@@ -181,3 +181,23 @@ def test_scales_that_are_not_staged():
     weights, v13, v2 = layer(r, 4, 128, 8192, "affine", 64)
     x, logits = inputs(r, 64, 128, 4, torch.float32)
     check(x, logits, weights, v13, v2, 2, "affine", 64)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("fmt,bs", FORMATS)
+@pytest.mark.parametrize("T", [1, 4, 40])
+def test_a_nan_or_an_infinity_is_not_lost(T, fmt, bs, dtype):
+    """A token with a NaN or an infinity gives NaN, whole; the other tokens' results stay within their bound."""
+    print(f"case moe NaN T={T} {fmt} {bs} {dtype}", flush=True)
+    r = np.random.default_rng(T + bs)
+    weights, v13, v2 = layer(r, 4, 256, 256, fmt, bs)
+    for value in (float("nan"), float("inf"), float("-inf")):
+        x, logits = inputs(r, T, 256, 4, dtype)
+        x[T // 2, 77] = value
+        got = q4.moe_q4(x, logits, *weights, 2, fmt=fmt, bs=bs)
+        assert got[T // 2].isnan().all()
+        keep = [t for t in range(T) if t != T // 2]
+        y, e = W.moe(W.as_f64(x)[keep], W.as_f64(logits)[keep], v13, v2, 2, bs, True)
+        if dtype == torch.bfloat16:
+            e = e + 2.0 ** -8 * (np.abs(y) + e)
+        assert (np.abs(W.as_f64(got)[keep] - y) <= e + 1e-30).all()
