@@ -294,8 +294,9 @@ __global__ __launch_bounds__(64 * WN* WM) void f8_tile_kernel(int M, int N, int 
 // QUANT: x itself comes in, and every workgroup quantizes it into LDS while
 // its first weights are on their way (one launch; taken for a few rows only,
 // since each workgroup repeats it).
-// 1 x 4096 x 4096 with the quantization inside: 6.0 us a call, 2.8 TB/s (a plain
-// read of 9.4 MB takes 3.2 us on this card, an empty launch 1.6).
+// 1 x 4096 x 4096 with the quantization inside: 6.0 us a call, 2.8 TB/s, weights
+// in the last-level cache (a kernel that only reads 16.8 MB takes 3.0 us there and
+// 3.9 from memory). 16 rows 9.1 us, 64 rows 14.5, both with the quantizer's launch.
 constexpr int ROWS_WAVES = 8;
 constexpr int ROWS_U = 4;  // blocks of k whose weights a wavefront has in flight
 
@@ -446,6 +447,8 @@ hipError_t launch_tiles(int M, int N, int KB, const uint8_t* xq, const float* xs
     // The largest tile that still gives every CU work: 256 x 256 moves the fewest bytes a product (4096 x 4096 x
     // 14336: 260 us), 128 x 128 fills the chip from 200 tiles on (1024 x 4096 x 4096: 25 us, against 34 with four
     // wavefronts a tile), 64 x 64 serves the rest (515 x 1500 x 1000 in float32: 7.7 us, against 15 with 128 x 128).
+    // The large and the middle tile take a CU's LDS, so 257 tiles are two waves of workgroups: 4096 x 4096 x 4096 (256
+    // tiles, quantizer included) 83 us, x 4352 (272 tiles) 128 us. The rule does not look at that.
     auto tiles = [&](long long tn, long long tm) { return ((N + tn - 1) / tn) * ((M + tm - 1) / tm); };
     // float32 results hold their operands as f16, twice the registers: no large tile
     if constexpr (YBF16)

@@ -13,7 +13,7 @@
 // order of tokens inside a sum is free), and V^T, stored [d][token], is read
 // with one 16-byte load for each 16 tokens of a d. No operand passes LDS.
 // Bound: the cache's bytes, read once: 64 sequences of 4096 to 16384 tokens, 8
-// key/value heads of 128, 289 us, 4.7 TB/s (a large copy moves 4.77 TB/s here). A
+// key/value heads of 128, 288 us, 4.7 TB/s (a large copy moves 4.77 TB/s here). A
 // long sequence is cut into splits, which a second launch joins: one sequence of
 // 1000 tokens 9.9 us, most of it launches and three dependent loads.
 //

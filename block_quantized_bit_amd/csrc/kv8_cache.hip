@@ -1,10 +1,12 @@
 // Storing into and reading from the 8-bit paged key/value cache (kv8.h).
 // One workgroup handles one page of one head of K or of V: it alone reads and
 // writes that page's codes and scale, so a scale that grows and the old codes'
-// rounding under the new one need no atomics. Both kernels are bound by memory
-// (or, for one token a sequence, by the launch): prompts of 13 000 tokens, 8 heads
-// of 128, 33 us to store (54 MB read, twice, the second time from a cache, 27 MB
-// written) and 16 us to read back (4.9 TB/s); 64 single tokens 5 us.
+// rounding under the new one need no atomics. Prompts of 13 000 tokens, 8 heads of
+// 128: 16 us to read back (4.9 TB/s, bound by memory), 33 us to store (54 MB read,
+// twice, the second time from a cache, 27 MB written; 17 us at a copy's rate). What
+// the storing waits for is not found: the second reading it is not, since keeping
+// the rows in registers took 32.6 us. 64 single tokens 5 us: the launch and loads
+// that depend on each other.
 #include <type_traits>
 
 #include "kernels_wide.h"

@@ -17,8 +17,8 @@
 // kernels, for 21 MB. Sixteen tokens, 2 of 8 experts (4096 x 14336, affine 128):
 // 224 us, 123 (3.9 TB/s) + 99 (2.4 TB/s). The second kernel's 99 us is the same
 // with v_dot4 or the matrix cores, with twice the loads in flight, with rotated
-// starts and with fewer cache lines a load: it waits for memory, the reason is
-// not found.
+// starts and with fewer cache lines a load: the reason is not found. (Not tried:
+// the tokens' codes in LDS, as in the first kernel.)
 #include <type_traits>
 
 #include "kernels_wide.h"
@@ -196,9 +196,9 @@ struct Piece {
     }
 };
 
-// acc over all pieces of the rows; `p` holds the first ones' loads. (A second set
-// of registers for the next pieces' loads halves the wavefronts of a CU, which
-// hide the loads better: 148 against 218 us for the batch of 16 tokens.)
+// acc over all pieces of the rows; `p` holds the first ones' loads. (No second set
+// of registers for the next pieces' loads: the wavefronts that a CU holds in their
+// place hide the loads.)
 template <int FMT, int G, int R, int LPR, int U, int NT, typename Act>
 __device__ __forceinline__ void row_products(Piece<FMT, G, R, LPR, U>& p, __amdgpu_buffer_rsrc_t rw,
                                              __amdgpu_buffer_rsrc_t rs, __amdgpu_buffer_rsrc_t rb,

@@ -62,8 +62,8 @@ typedef struct {
  *   s     = s_new if the page's first new token is in slot 0, else max(the page's scale, s_new)
  *   codes of tokens that the page held before: round(c * (s_old / s)) where s grew (s_old / s and the product in
  *   float32), unchanged otherwise; new codes: round(x / s) with the float32 quotient, cut at +-L; 0 where s is 0
- * (round: half to even, to an integer or to an e4m3 value). A NaN is stored as 0 and an infinity as the largest
- * finite float32, so that one bad value does not spoil the page's other tokens.
+ * (round: half to even, to an integer or to an e4m3 value). A NaN is stored as 0, an infinity as the largest finite
+ * float32: codes and scales stay finite. (The page's scale is then 2^120 or so, under which ordinary values are 0.)
  */
 int kv8_append(const kv8_cache* cache, int total, int max_new, int dtype, const void* k_new, long long k_stride,
                const void* v_new, long long v_stride, void* stream);

@@ -18,8 +18,10 @@
  * Layouts (codes, scales and formats of q4.h, bits = 4):
  *   w13 [E][2 I][H/2] codes: rows 0 .. I-1 of an expert are W1 (gate), rows I .. 2I-1 W3 (up);
  *   s13, b13 [E][2 I][H/bs];  w2 [E][H][I/2];  s2, b2 [E][H][I/bs]
- * Only the chosen experts' weights are read, once each for up to 8 of an
- * expert's tokens.
+ * Only the chosen experts' weights are read, W1 and W3 once for each 4 to 16 of
+ * an expert's tokens (about twice the mean number of an expert, as far as their
+ * codes fit a CU's LDS; 1 for very long rows), W2 once for each 8, or 16 on the
+ * matrix cores.
  *
  * Conventions (pointers, streams, workspaces, statuses) are those of q4.h.
  */
