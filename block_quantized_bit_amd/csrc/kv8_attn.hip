@@ -2,7 +2,8 @@
 //
 // A query row is a (token, head of the group) pair of one key/value head; a
 // tile of 16 RT rows shares every key and value byte it reads. A wavefront
-// works on chunks of 64 tokens with v_mfma_f32_16x16x32_f16:
+// works on chunks of 64 tokens with v_mfma_f32_16x16x32_f16 (for float32 results the
+// second product is v_mfma_f32_16x16x32_bf16):
 //   S^T = K Q^T   A = keys (rows: tokens), B = queries (columns)
 //   O^T = V^T P^T A = V^T (rows: d), B = probabilities (columns: queries)
 // Column r of both results belongs to lane r (mod 16), so the softmax runs
@@ -506,11 +507,12 @@ __global__ __launch_bounds__(256) void kv8_attn_kernel(Kv8 c, Attend a) {
 // ---- many rows ------------------------------------------------------------------------
 // Prompts and chunks of prompts: bound by the matrix cores and by the softmax's
 // VALU work, not by the cache's bytes, so the four wavefronts of a workgroup
-// (16 RT rows each) share every chunk: it is converted to f16 once, a quarter by
-// each wavefront, and the operands come from LDS, two chunks alternating. A
+// (16 RT rows each) share every chunk: it is converted to the products' 16-bit
+// types once, a quarter by each wavefront, and the operands come from LDS, two
+// chunks alternating. A
 // thread's codes of the next chunk are loaded before the current one is used
 // and converted after it.
-// LDS: a key is a row of D f16 in 16-byte pieces, a value row (one d) has its 64
+// LDS: a key is a row of D values in 16-byte pieces, a value row (one d) has its 64
 // tokens in eight, those of step 0 first. Pieces are stored at piece ^ key, where
 // the key of a token is its row in the first product and that of a value row half
 // its number, so that the sixteen lanes that a 16-byte read serves at once, which
