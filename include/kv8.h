@@ -82,10 +82,11 @@ size_t kv8_attention_work_bytes(const kv8_cache* cache, int total, int max_new, 
  * over the positions t <= that of the query, with window > 0 only the last `window` of them, and t < max_kv. A query
  * that sees no key gives zeros. out [total][heads][D] in q's dtype, contiguous. lse [total][heads] float32 may be
  * NULL: log(sum_t exp(scale * q . k_t)), -infinity for a query that sees no key. A query with a NaN gives NaN in both.
- * Softmax statistics and sums are float32, and codes enter the products exactly. For float32 results queries enter as
- * two f16 halves (22 bits of the row's largest value) and weights p_t in full. For bfloat16 results queries are exact
- * (22 bits of the row's largest value) and a weight is rounded to f16's eleven bits, or to 2^-36 of the largest one.
- * (Where all value scales lie below 2^-80, say at 2^(-80 - k), that is 2^(k - 36) of the largest one.)
+ * Softmax statistics and sums are float32, and codes enter the products exactly. A token's weight is p_t times its
+ * page's value scale. For float32 results queries enter as two f16 halves (22 bits of the row's largest value) and
+ * weights in full. For bfloat16 results queries are exact (22 bits of the row's largest value) and a weight is rounded
+ * to f16's eleven bits, or to 2^-36 of the row's largest weight (to 2^(k - 36) of it where no value scale is above
+ * 2^(-80 - k)): a page whose value scale is 2^36 times another's hides that one's values.
  */
 int kv8_attention(const kv8_cache* cache, int total, int max_new, int max_kv, int heads, int dtype, const void* q,
                   long long q_stride, float scale, int window, void* out, float* lse, void* work, void* stream);
